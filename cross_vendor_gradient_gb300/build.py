@@ -18,7 +18,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["gb_kernels_enc.cu", "gb_kernels_dec.cu", "gb_kernels_exact.cu", "gb_runtime.cu", "gb_api.cu",
            "gb_noalloc.cu", "gb_kernels_adamw.cu", "gb_kernels_rms.cu", "gb_train_api.cu"]
 HEADERS = [os.path.join(INCLUDE, "gb.h")] + [
-    os.path.join(CSRC, f) for f in ("gb_device.cuh", "gb_kernels.cuh", "gb_internal.cuh", "gb_train.cuh")]
+    os.path.join(CSRC, f) for f in ("gb_device.cuh", "gb_kernels.cuh", "gb_internal.cuh", "gb_train.cuh", "gb_rows.cuh")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]

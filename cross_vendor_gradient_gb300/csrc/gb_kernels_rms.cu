@@ -14,45 +14,12 @@
 // output.
 #include <atomic>
 
+#include "gb_rows.cuh"
 #include "gb_train.cuh"
 
 namespace gb {
 
 // ------------------------------------------------------------------- rows
-// A row's elements start at any element, and the buffers at 16 bytes.  Row
-// tensors of one shape share their offsets, so a team of threads covers a row
-// from the vector boundary at or before its first element, `skew` elements
-// ahead: vector v of thread i has elements p - skew .. p - skew + 7 of the
-// row, p = 8 (i + v team).  A team is a power of two of a warp's lanes for
-// short rows, else whole warps, one team a block (in the forward kernel), and
-// its rows lie a multiple of 8 apart: the skew, and with it what each thread
-// has, stays the same from row to row.
-constexpr int kMaxTeam = 512;
-
-template <int V> struct Mine {
-    int skew, lo, hi;    // its end vectors' own parts: [lo, 8) of the first, [0, hi) of the last
-    uint32_t has;        // bit v: some of vector v is the row's
-    uint32_t head, tail; // bit v: but not all of it, at the row's start / end
-};
-template <int V>
-__device__ __forceinline__ Mine<V> mine_of(uint64_t row, uint32_t cols, int i, int team) {
-    Mine<V> m{(int)(row * cols & 7), 0, 8, 0, 0, 0};
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int pos = 8 * (i + v * team), lo = m.skew - pos, hi = m.skew + (int)cols - pos;
-        if (hi <= 0) continue;
-        m.has |= 1u << v;
-        if (lo > 0) {
-            m.head |= 1u << v;
-            m.lo = lo;
-        }
-        if (hi < 8) {
-            m.tail |= 1u << v;
-            m.hi = hi;
-        }
-    }
-    return m;
-}
 // The own part of vector v.
 template <int V> __device__ __forceinline__ int own_lo(const Mine<V> &m, int v) { return m.head >> v & 1 ? m.lo : 0; }
 template <int V> __device__ __forceinline__ int own_hi(const Mine<V> &m, int v) { return m.tail >> v & 1 ? m.hi : 8; }
@@ -135,18 +102,19 @@ __device__ __forceinline__ void keep_own(Raw8<T> &r, int lo, int hi) {
 // A thread's vectors of a row, the row's boundary at element `at`.  With a
 // skew the end vectors are read whole, with elements of the rows beside this
 // one (which another team may be overwriting in place; they are not used);
-// only the tensor's last vector, if it is cut, goes element by element.
+// in a row that is `cut` the last vector reaches beyond the tensor's end, and
+// goes element by element.
 template <typename T, int V, bool WIDE, bool SKEW>
 __device__ __forceinline__ void load_row(Raw8<T> x[V], const T *tensor, uint64_t at, const Mine<V> &m, int i, int team, bool row,
-                                         bool last) {
+                                         bool cut) {
     const T *const p = tensor + at + 8 * i;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const uint32_t whole = SKEW && last ? m.has & ~m.tail : m.has;
+        const uint32_t whole = whole_vectors<V>(m, SKEW && cut);
         x[v] = load_vector<T, WIDE>(p + 8 * v * team, row && (whole >> v & 1));
     }
     if constexpr (SKEW) {
-        if (!last || !m.tail) return;
+        if (!cut || !m.tail) return;
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (m.tail >> v & 1) {
@@ -298,9 +266,9 @@ __global__ void __launch_bounds__(kMaxTeam) k_rms_norm(const __grid_constant__ R
     Raw8<T> w[V], x[V], res[V];
     load_weights<T, V, WIDE, SKEW>(w, (const T *)a.weight, m, i, team, a.cols);
     auto load = [&]() {
-        load_row<T, V, WIDE, SKEW>(x, (const T *)a.x, at, m, i, team, row < a.rows, row + 1 == a.rows);
-        if (a.residual)
-            load_row<T, V, WIDE, SKEW>(res, (const T *)a.residual, at, m, i, team, row < a.rows, row + 1 == a.rows);
+        const bool valid = row < a.rows, cut = row - a.whole_rows < a.rows - a.whole_rows;  // whole_rows <= row < rows
+        load_row<T, V, WIDE, SKEW>(x, (const T *)a.x, at, m, i, team, valid, cut);
+        if (a.residual) load_row<T, V, WIDE, SKEW>(res, (const T *)a.residual, at, m, i, team, valid, cut);
     };
     if (kAhead) load();
     int parity = 0;
@@ -514,10 +482,10 @@ __global__ void __launch_bounds__(kMaxTeam) k_rms_grad(const __grid_constant__ R
     float acc[V][8] = {}, rstd = 0.0f;
     load_weights<T, V, WIDE, SKEW>(w, (const T *)a.weight, m, i, team, a.cols);
     auto load = [&]() {
-        const bool valid = row < a.rows, last = row + 1 == a.rows;
-        load_row<T, V, WIDE, SKEW>(dy, (const T *)a.dy, at, m, i, team, valid, last);
-        load_row<T, V, WIDE, SKEW>(h, (const T *)a.h, at, m, i, team, valid, last);
-        if (kAheadSum && a.dsum) load_row<T, V, WIDE, SKEW>(ds, (const T *)a.dsum, at, m, i, team, valid, last);
+        const bool valid = row < a.rows, cut = valid && row >= a.whole_rows;
+        load_row<T, V, WIDE, SKEW>(dy, (const T *)a.dy, at, m, i, team, valid, cut);
+        load_row<T, V, WIDE, SKEW>(h, (const T *)a.h, at, m, i, team, valid, cut);
+        if (kAheadSum && a.dsum) load_row<T, V, WIDE, SKEW>(ds, (const T *)a.dsum, at, m, i, team, valid, cut);
         rstd = valid ? a.rstd[row] : 0.0f;
     };
     if (kAhead) load();
@@ -529,7 +497,7 @@ __global__ void __launch_bounds__(kMaxTeam) k_rms_grad(const __grid_constant__ R
         const float scale = rstd;
         float s[8] = {};
         Raw8<T> this_dy[V], this_h[V], d[V];  // dy and h stay packed across the barrier
-        if (!kAheadSum && a.dsum) load_row<T, V, WIDE, SKEW>(d, (const T *)a.dsum, at, m, i, team, valid, row + 1 == a.rows);
+        if (!kAheadSum && a.dsum) load_row<T, V, WIDE, SKEW>(d, (const T *)a.dsum, at, m, i, team, valid, valid && row >= a.whole_rows);
         if constexpr (SKEW) {
             cut_row<T, V>(dy, m);
             cut_row<T, V>(h, m);
@@ -642,17 +610,6 @@ __global__ void __launch_bounds__(kRowThreads) k_rms_dx_elements(const __grid_co
 }
 
 // ----------------------------------------------------------------- launch
-// Threads of a team with V vectors each that hold a row of cols elements (and
-// its skew); 0 if that is more than kMaxTeam.
-static int team_of(uint32_t cols, int V) {
-    const uint64_t need = ((uint64_t)cols + (cols % 8 ? 7 : 0) + 8 * V - 1) / (8 * V);
-    if (need > kMaxTeam) return 0;
-    if (V > 1 || need > 32) return (int)(need + 31) / 32 * 32;
-    int t = 1;
-    while ((uint64_t)t < need) t *= 2;
-    return t;
-}
-
 // Blocks of `threads` threads and `shared` dynamic bytes of a kernel that one
 // SM holds; the runtime is asked when they are not those of the last call.
 template <auto Kern>

@@ -97,7 +97,7 @@ struct RmsArgs {
     const void *x, *residual, *weight;
     void *sum, *out;
     float *rstd;
-    uint64_t rows;
+    uint64_t rows, whole_rows;
     uint32_t cols;
     float eps, inv_cols;
     uint64_t scales_off;  // 8-bit output: byte offset of the scales
@@ -109,7 +109,7 @@ struct RmsGradArgs {
     void *dx, *dweight;
     float *partials;  // [n_partials, cols]
     int n_partials;  // set by the launcher
-    uint64_t rows;
+    uint64_t rows, whole_rows;
     uint32_t cols;
     float inv_cols;
     int team;  // threads per row, set by the launcher

@@ -3,6 +3,7 @@
 #include <cmath>
 
 #include "gb_internal.cuh"
+#include "gb_rows.cuh"
 #include "gb_train.cuh"
 
 using namespace gbrt;
@@ -266,6 +267,7 @@ gb_status gb_rms_norm(gb_ctx *c, const void *x, const void *residual, const void
     a.out = out;
     a.rstd = rstd;
     a.rows = rows;
+    a.whole_rows = gb::whole_rows(rows, (uint32_t)cols);
     a.cols = (uint32_t)cols;
     a.eps = eps;
     a.inv_cols = 1.0f / (float)cols;
@@ -312,6 +314,7 @@ gb_status gb_rms_norm_backward(gb_ctx *c, const void *dy, const void *h, const v
     a.dweight = dweight;
     a.partials = (float *)(c->d_work + gb::kWorkHead);
     a.rows = rows;
+    a.whole_rows = gb::whole_rows(rows, (uint32_t)cols);
     a.cols = (uint32_t)cols;
     a.inv_cols = 1.0f / (float)cols;
     GB_TRY(check_launch(c, gb::launch_rms_norm_backward(a, dtype, s), "RMS norm gradient"));
