@@ -43,6 +43,7 @@ gb_status gb_destroy(gb_ctx *c) {
         if (c->d_work) cudaFree(c->d_work);
         if (c->h_stage) cudaFreeHost(c->h_stage);
         if (c->done) cudaEventDestroy(c->done);
+        if (c->work_done) cudaEventDestroy(c->work_done);
         drop_graphs(c);
         free_marks(c);
         cudaStream_t streams[4] = {c->sd, c->sh, c->scap, c->sg};

@@ -75,9 +75,15 @@ struct gb_ctx {
     // device copies of host rank buffers (gb_all_reduce_host)
     unsigned char *d_ranks = nullptr;
     size_t d_ranks_bytes = 0;
-    // fixed workspace of the calls that join partial sums (gb_train_api.cu)
+    // fixed workspace of the calls that join partial sums (gb_train_api.cu),
+    // and the order of those being captured
     unsigned char *d_work = nullptr;
     size_t d_work_bytes = 0;
+    bool work_ready = false;
+    uint32_t work_tickets = 0;            // captured calls so far
+    unsigned long long work_capture = 0;  // the last one's capture, stream and event
+    cudaStream_t work_stream = nullptr;
+    cudaEvent_t work_done = nullptr;
     size_t max_pitch = 0;  // cudaDevAttrMaxPitch of the bound device (2D copies)
     // ordering of staging reuse across calls
     cudaEvent_t done = nullptr;

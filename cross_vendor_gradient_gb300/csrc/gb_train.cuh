@@ -43,12 +43,13 @@ inline uint32_t vector_shift(const void *p, size_t eb) { return (uint32_t)(((uin
 // Tiles of a tensor whose first tile starts `shift` elements before element 0.
 inline uint64_t tiles_of(uint64_t n, uint32_t shift, uint32_t tile) { return (n + shift + tile - 1) / tile; }
 
-// Device workspace of a context, for the calls that join partial sums: a
-// ticket counter, then float64 or float32 partials.  One fixed allocation,
-// made by the first such call and kept: a captured call's pointers stay good.
-constexpr size_t kWorkHead = 256;
+// Device workspace of a context, for the calls that join partial sums: ticket
+// counters (the eager calls' one, then one for each captured call, in turn),
+// then float64 or float32 partials of the eager calls and of the captured
+// ones.  One fixed allocation, made by the first such call and kept: a
+// captured call's pointers stay good.
+constexpr size_t kWorkHead = 64u << 10;
 constexpr size_t kWorkFloats = 8u << 20;
-constexpr size_t kWorkBytes = kWorkHead + 4 * kWorkFloats;
 
 template <int N> struct NormArgs {
     double *partials;    // one per block of every launch of the call

@@ -37,26 +37,51 @@ gb_status check_tensors(gb_ctx *c, int n_tensors, const size_t *numel, uint64_t 
     return GB_OK;
 }
 
-gb_status is_capturing(gb_ctx *c, cudaStream_t s, bool *yes) {
+// A call's use of the context's workspace: a ticket counter, zero between
+// calls, and partial sums.
+struct Work {
+    unsigned long long capture = 0;  // id of the capture that the stream is in; 0: none
+    uint32_t *ticket = nullptr;
+    unsigned char *partials = nullptr;
+};
+
+// A call outside of captures is ordered after the previous call that used
+// staging.  Captured calls have partial sums of their own, since their graph
+// may run next to later calls; those of one capture are ordered after each
+// other, also on parallel branches.  Each captured call has a ticket of its
+// own: two graphs that ran at the same time, against the rule, would spoil
+// each other's sums, but leave no count behind.
+gb_status begin_work(gb_ctx *c, cudaStream_t s, Work *w) {
     cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    const cudaError_t e = cudaStreamIsCapturing(s, &st);
-    if (e != cudaSuccess) return fail(c, GB_ERR_CUDA, "cudaStreamIsCapturing", e);
-    *yes = st != cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    cudaError_t e = cudaStreamGetCaptureInfo(s, &st, &id);
+    if (e != cudaSuccess) return fail(c, GB_ERR_CUDA, "cudaStreamGetCaptureInfo", e);
+    w->capture = st == cudaStreamCaptureStatusNone ? 0 : id;
+    if (!c->work_ready) {
+        if (w->capture) return set_msg(c, GB_ERR_INVALID_ARG, "the first call that needs the workspace is being captured");
+        GB_TRY(grow_device(c, &c->d_work, &c->d_work_bytes, gb::kWorkHead + 2 * 4 * gb::kWorkFloats));
+        if ((e = cudaEventCreateWithFlags(&c->work_done, cudaEventDisableTiming)) != cudaSuccess)
+            return fail(c, GB_ERR_CUDA, "cudaEventCreate", e);
+        // complete before any stream's call: graphs run on streams that are not known here
+        if ((e = cudaMemsetAsync(c->d_work, 0, gb::kWorkHead, c->sg)) != cudaSuccess || (e = cudaStreamSynchronize(c->sg)) != cudaSuccess)
+            return fail(c, GB_ERR_CUDA, "clearing the workspace", e);
+        c->work_ready = true;
+    }
+    w->ticket = (uint32_t *)c->d_work;
+    w->partials = c->d_work + gb::kWorkHead;
+    if (!w->capture) return begin(c, s);
+    w->ticket += 1 + c->work_tickets++ % (gb::kWorkHead / sizeof(uint32_t) - 1);
+    w->partials += 4 * gb::kWorkFloats;
+    if (c->work_capture == w->capture && c->work_stream != s) GB_TRY(wait_on(c, s, c->work_done));
     return GB_OK;
 }
-
-// The context's workspace, ordered after the previous call that used staging.
-gb_status begin_work(gb_ctx *c, cudaStream_t s, bool *capturing) {
-    GB_TRY(is_capturing(c, s, capturing));
-    if (!c->d_work) {
-        if (*capturing) return set_msg(c, GB_ERR_INVALID_ARG, "the first call that needs the workspace is being captured");
-        GB_TRY(grow_device(c, &c->d_work, &c->d_work_bytes, gb::kWorkBytes));
-        const cudaError_t e = cudaMemsetAsync(c->d_work, 0, gb::kWorkHead, s);
-        if (e != cudaSuccess) return fail(c, GB_ERR_CUDA, "cudaMemsetAsync", e);
-    }
-    return *capturing ? GB_OK : begin(c, s);
+gb_status end_work(gb_ctx *c, cudaStream_t s, const Work &w) {
+    if (!w.capture) return end(c, s);
+    GB_TRY(record(c, c->work_done, s));
+    c->work_capture = w.capture;
+    c->work_stream = s;
+    return GB_OK;
 }
-gb_status end_work(gb_ctx *c, cudaStream_t s, bool capturing) { return capturing ? GB_OK : end(c, s); }
 
 // Whether [a, a + na) and [b, b + nb) overlap without starting together.
 bool cross(const void *a, size_t na, const void *b, size_t nb) {
@@ -68,11 +93,11 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) { return a && (
 
 // The launches of a norm, N tensors each.
 template <int N>
-gb_status norm_launches(gb_ctx *c, int n_tensors, const void *const *grads, const size_t *numel, gb_dtype dtype, float max_norm,
-                        float *out, cudaStream_t s) {
+gb_status norm_launches(gb_ctx *c, const Work &w, int n_tensors, const void *const *grads, const size_t *numel, gb_dtype dtype,
+                        float max_norm, float *out, cudaStream_t s) {
     gb::NormArgs<N> a;
-    a.ticket = (uint32_t *)c->d_work;
-    a.partials = (double *)(c->d_work + gb::kWorkHead);
+    a.ticket = w.ticket;
+    a.partials = (double *)w.partials;
     a.out = out;
     a.max_norm = max_norm;
     uint32_t used = 0;
@@ -171,13 +196,13 @@ gb_status gb_grad_norm(gb_ctx *c, int n_tensors, const void *const *grads, const
     GB_TRY(check_align(c, out, 4, "out"));
     GB_TRY(bind(c));
     cudaStream_t s = (cudaStream_t)stream;
-    bool capturing = false;
-    GB_TRY(begin_work(c, s, &capturing));
+    Work w;
+    GB_TRY(begin_work(c, s, &w));
     int filled = 0;
     for (int t = 0; t < n_tensors; ++t) filled += numel[t] != 0;
-    GB_TRY(filled <= gb::kFewTensors ? norm_launches<gb::kFewTensors>(c, n_tensors, grads, numel, dtype, max_norm, out, s)
-                                     : norm_launches<gb::kNormTensors>(c, n_tensors, grads, numel, dtype, max_norm, out, s));
-    return end_work(c, s, capturing);
+    GB_TRY(filled <= gb::kFewTensors ? norm_launches<gb::kFewTensors>(c, w, n_tensors, grads, numel, dtype, max_norm, out, s)
+                                     : norm_launches<gb::kNormTensors>(c, w, n_tensors, grads, numel, dtype, max_norm, out, s));
+    return end_work(c, s, w);
 }
 
 gb_status gb_adamw_step(gb_ctx *c, int n_tensors, float *const *params, const void *const *grads,
@@ -302,8 +327,8 @@ gb_status gb_rms_norm_backward(gb_ctx *c, const void *dy, const void *h, const v
         return set_msg(c, GB_ERR_INVALID_ARG, "buffers overlap");
     GB_TRY(bind(c));
     cudaStream_t s = (cudaStream_t)stream;
-    bool capturing = false;
-    GB_TRY(begin_work(c, s, &capturing));
+    Work work;
+    GB_TRY(begin_work(c, s, &work));
     gb::RmsGradArgs a;
     a.dy = dy;
     a.h = h;
@@ -312,13 +337,13 @@ gb_status gb_rms_norm_backward(gb_ctx *c, const void *dy, const void *h, const v
     a.rstd = rstd;
     a.dx = dx;
     a.dweight = dweight;
-    a.partials = (float *)(c->d_work + gb::kWorkHead);
+    a.partials = (float *)work.partials;
     a.rows = rows;
     a.whole_rows = gb::whole_rows(rows, (uint32_t)cols);
     a.cols = (uint32_t)cols;
     a.inv_cols = 1.0f / (float)cols;
     GB_TRY(check_launch(c, gb::launch_rms_norm_backward(a, dtype, s), "RMS norm gradient"));
-    return end_work(c, s, capturing);
+    return end_work(c, s, work);
 }
 
 }  // extern "C"

@@ -593,12 +593,15 @@ gb_status gb_all_reduce_noalloc(gb_ctx *ctx, void *const *rank_bufs, size_t n, g
  * BF16, F16 (GB_ERR_UNSUPPORTED_DTYPE otherwise); all arithmetic is float32.
  * They run on the caller's stream like every other call.  gb_adamw_step and
  * gb_rms_norm use no memory of the context and may be captured into a CUDA
- * graph.  gb_grad_norm and gb_rms_norm_backward use a fixed workspace of the
- * context (32 MiB, allocated by the first such call, kept until gb_destroy)
- * and are ordered with the context's other calls; they may be captured once
- * the workspace exists (GB_ERR_INVALID_ARG before), and a captured call is
- * then ordered by the streams that its graph is launched on alone.  Their
- * results do not change from run to run. */
+ * graph.  gb_grad_norm and gb_rms_norm_backward use fixed workspaces of the
+ * context (two of 32 MiB, allocated by the first such call, kept until
+ * gb_destroy) and are ordered with the context's other calls; they may be
+ * captured once the workspaces exist (GB_ERR_INVALID_ARG before).  Captured
+ * calls share the second workspace: those of one capture are ordered after
+ * each other, on parallel branches too, and a graph may run next to calls
+ * outside of graphs.  Two captures with such calls of one context must not be
+ * in progress, nor their graphs run, at the same time.  Results do not change
+ * from run to run. */
 
 /* The 2-norm of all gradients together, and the factor that clips them:
  *   out[0] = norm = sqrt(sum of g^2 over the n_tensors tensors),
