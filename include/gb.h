@@ -606,9 +606,12 @@ gb_status gb_all_reduce_noalloc(gb_ctx *ctx, void *const *rank_bufs, size_t n, g
 /* The 2-norm of all gradients together, and the factor that clips them:
  *   out[0] = norm = sqrt(sum of g^2 over the n_tensors tensors),
  *   out[1] = factor = min(1, max_norm / (norm + 1e-6)); 1 when
- *            max_norm <= 0 (no clipping); NaN when norm is not finite (a
- *            gradient is infinite or NaN, or beyond 1.8e19, whose square
- *            float32 does not hold), which gb_adamw_step refuses.
+ *            max_norm <= 0 (no clipping); NaN when norm is not finite, which
+ *            gb_adamw_step refuses.
+ * norm is infinite where a gradient is infinite, or beyond 1.8e19 (its square
+ * is beyond float32), NaN where one is NaN; of all others, down to the
+ * smallest subnormal and whatever their number, it is right within a few
+ * roundings of float32.
  * grads: n_tensors device tensors of numel[t] elements, aligned to their
  * element (tensors packed into a bucket without gaps); entries of no
  * elements may be NULL.  out: 2 floats, device.  With no elements at all the
