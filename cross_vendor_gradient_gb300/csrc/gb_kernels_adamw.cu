@@ -558,9 +558,9 @@ __device__ __forceinline__ void store_shifted(T *tensor, int64_t base, int lane,
 template <typename T, bool COPY, int N>
 __global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ AdamwArgs<N> a) {
     const int lane = threadIdx.x & 31;
-    const uint32_t stride = gridDim.x * 8;
-    uint32_t tile = blockIdx.x * 8 + (threadIdx.x >> 5) + wait_prior_grid();
-    const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
+    const uint32_t stride = gridDim.x * 8, zero = wait_prior_grid();
+    uint32_t tile = blockIdx.x * 8 + (threadIdx.x >> 5) + zero;
+    const float scale = a.grad_scale ? a.grad_scale[zero] : 1.0f;  // the kernel before this one may write it
     if (!isfinite(scale)) return;  // the step is refused: nothing changes
     Place q;
     q.end = 0;
