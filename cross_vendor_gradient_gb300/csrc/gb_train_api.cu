@@ -55,7 +55,12 @@ gb_status begin_work(gb_ctx *c, cudaStream_t s, Work *w) {
     cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
     unsigned long long id = 0;
     cudaError_t e = cudaStreamGetCaptureInfo(s, &st, &id);
+    if (e == cudaErrorStreamCaptureImplicit) {  // nothing has been enqueued: the context stays sound
+        cudaGetLastError();
+        return set_msg(c, GB_ERR_INVALID_ARG, "the legacy stream, while a stream that synchronizes with it is being captured");
+    }
     if (e != cudaSuccess) return fail(c, GB_ERR_CUDA, "cudaStreamGetCaptureInfo", e);
+    if (st == cudaStreamCaptureStatusInvalidated) return set_msg(c, GB_ERR_INVALID_ARG, "the stream's capture has been invalidated");
     w->capture = st == cudaStreamCaptureStatusNone ? 0 : id;
     if (!c->work_ready) {
         if (w->capture) return set_msg(c, GB_ERR_INVALID_ARG, "the first call that needs the workspace is being captured");

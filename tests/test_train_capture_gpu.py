@@ -1,9 +1,12 @@
 """The training-step operators in CUDA graphs: calls that share the context's workspace on parallel branches of one
 graph, next to calls outside of it, and what a capture refuses."""
+import ctypes
+
 import pytest
 import torch
 
-from cross_vendor_gradient_gb300 import Context
+from cross_vendor_gradient_gb300 import Context, GbError
+from cross_vendor_gradient_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +119,68 @@ def test_one_capture_after_another(ctx):
     for g, o in zip(sets, outs):
         want = float(g.double().norm())
         assert abs(o[0].item() - want) < 1e-6 * want
+
+
+class DriverStream:
+    """A stream that synchronizes with the legacy stream, which torch's streams do not, and its capture."""
+
+    def __init__(self):
+        self.cu, self.handle, self.graph = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p(), ctypes.c_void_p()
+        assert self.cu.cuStreamCreate(ctypes.byref(self.handle), 0) == 0
+
+    @property
+    def cuda_stream(self):
+        return self.handle.value
+
+    def begin(self):
+        assert self.cu.cuStreamBeginCapture_v2(self.handle, 1) == 0  # thread local
+
+    def end(self):
+        status = self.cu.cuStreamEndCapture(self.handle, ctypes.byref(self.graph))
+        if self.graph:
+            self.cu.cuGraphDestroy(self.graph)
+        return status
+
+    def destroy(self):
+        self.cu.cuStreamDestroy_v2(self.handle)
+
+
+def test_the_legacy_stream_during_a_capture_is_refused(ctx):
+    """The call is refused, the capture goes on, and the context stays usable."""
+    x, out = torch.full((1000,), 2.0, device="cuda"), torch.zeros(2, device="cuda")
+    rows = Rows(1, 10, 64)
+    ctx.grad_norm([x], out)
+    torch.cuda.synchronize()
+    other = DriverStream()
+    legacy = torch.cuda.default_stream()
+    assert legacy.cuda_stream == 0
+    other.begin()
+    for call in (lambda: ctx.grad_norm([x], out, stream=legacy), lambda: rows.run(ctx, stream=legacy)):
+        with pytest.raises(GbError) as e:
+            call()
+        assert e.value.status == B.GB_ERR_INVALID_ARG
+    ctx.grad_norm([x], out, stream=other)
+    assert other.end() == 0
+    assert ctx.status() == B.GB_OK
+    out.zero_()
+    ctx.grad_norm([x], out, stream=legacy)
+    torch.cuda.synchronize()
+    assert abs(out[0].item() - 4000 ** 0.5) < 1e-5
+    other.destroy()
+
+
+def test_a_capture_that_has_been_invalidated_is_refused(ctx):
+    x, out = torch.ones(1000, device="cuda"), torch.zeros(2, device="cuda")
+    ctx.grad_norm([x], out)
+    torch.cuda.synchronize()
+    other = DriverStream()
+    other.begin()
+    assert other.cu.cuStreamSynchronize(other.handle) != 0  # not allowed in a capture: an error, and no capture any more
+    with pytest.raises(GbError) as e:
+        ctx.grad_norm([x], out, stream=other)
+    assert e.value.status == B.GB_ERR_INVALID_ARG and ctx.status() == B.GB_OK
+    assert other.end() != 0
+    ctx.grad_norm([x], out)
+    torch.cuda.synchronize()
+    assert abs(out[0].item() - 1000 ** 0.5) < 1e-5
+    other.destroy()
