@@ -439,7 +439,8 @@ class AdamW:
     The tensors are checked, and their addresses taken, once: a step costs one
     call whatever their number.  Parameters, gradients and copies stay where
     they are (views into gradient buckets, for instance); the states are
-    exp_avg / exp_avg_sq, made here (zero) unless given.
+    exp_avg / exp_avg_sq, made here (zero) unless given: the host then waits
+    until they are, so that a step may run on any stream.
     """
 
     def __init__(self, ctx, params, grads, exp_avg=None, exp_avg_sq=None, copies=None, lr=1e-3, betas=(0.9, 0.999),
@@ -468,6 +469,8 @@ class AdamW:
                 raise GbError(B.GB_ERR_INVALID_ARG, "%s: %d tensors for %d parameters" % (name, len(ts), len(numel)))
             for t, n in zip(ts, counts):
                 _expect(t, dtype, n, name, device)
+        if (exp_avg is None or exp_avg_sq is None) and self.params and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(device).synchronize()
         self._arrays = [None if ts is None else B._ptrs([t.data_ptr() for t in ts])
                         for ts in (self.params, self.grads, self.exp_avg, self.exp_avg_sq, self.copies)]
         self._numel = B._sizes(numel)

@@ -37,3 +37,20 @@ def test_a_step_takes_the_factor_of_the_norm_just_before_it(ctx, states):
         runs.append((p, opt.exp_avg[0], opt.exp_avg_sq[0]))
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("states", ["none", "e4m3"])
+def test_states_made_by_the_optimizer_are_zero_before_a_step_on_another_stream(ctx, states):
+    """The current stream is busy when the optimizer is made, the first step runs on another one."""
+    p, grad = torch.zeros(3000, device="cuda"), torch.ones(3000, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    opt = ctx.adamw([p], [grad], states=states, lr=0.1, weight_decay=0.0, betas=(0.5, 0.5))
+    opt.step(stream=side)
+    torch.cuda.synchronize()
+    if states == "none":
+        assert bool((opt.exp_avg[0] == 0.5).all()) and bool((opt.exp_avg_sq[0] == 0.5).all())
+    else:
+        assert bool((opt.exp_avg[0][:3000] != 0).all()) and bool((opt.exp_avg_sq[0][:3000] != 0).all())
+    assert bool(((p + 0.1).abs() < 1e-6).all())  # 0.1 m / (1 - 0.5) / (sqrt(v / (1 - 0.5)) + eps), m = v = 0.5
