@@ -42,6 +42,16 @@ def _stream(stream=None):
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())  # current_stream() without its Stream object
 
 
+def _capturing(stream):
+    """Whether the stream (None: the current one) is being captured together with the current one."""
+    if not torch._C._cuda_isCurrentStreamCapturing():  # torch.cuda.is_current_stream_capturing(), half its time
+        return False
+    if stream is None:
+        return True
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _dtype(tensors):
     dt = tensors[0].dtype
     if dt not in _DTYPES:
@@ -480,8 +490,14 @@ class AdamW:
         """One step, from the gradients as they are now.  step: its number
         (default: one more than the last; a step that the device refuses for
         a grad_scale that is not finite counts too); seed: of the 8-bit
-        states' random numbers."""
-        step = self.steps + 1 if step is None else step
+        states' random numbers.  The number, the seed and the learning rate
+        are taken at the call: a graph repeats them in every replay, and with
+        them the bias correction and the random numbers, so a captured step
+        has to be given its number."""
+        if step is None:
+            if _capturing(stream):
+                raise GbError(B.GB_ERR_INVALID_ARG, "a captured step needs its number, which every replay repeats")
+            step = self.steps + 1
         if grad_scale is not None:
             _expect(grad_scale, torch.float32, 1, "grad_scale")
         cfg = B.Adamw(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, step, seed)

@@ -655,6 +655,11 @@ typedef struct {
  *       still.)  A v of 2^-129 or more is never coded as zero.  Infinities and NaN
  *       are coded as NaN, and leave their block's scale alone.
  *     Other codecs: GB_ERR_UNSUPPORTED_CODEC.
+ * cfg is read at the call.  A captured call therefore repeats its step in
+ * every replay of the graph: the same bias correction, learning rate and
+ * random numbers (so that 8-bit states are rounded at the same threshold
+ * each time, and a slow average may stand still).  To train by a graph,
+ * capture the step anew, or update its kernel node, for each step.
  * params, grads, copies and float32 states need the alignment of their
  * element only; tensors must not overlap each other.  Streaming at full rate
  * wants all of a tensor's arrays at the same distance, in elements, from a

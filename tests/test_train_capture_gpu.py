@@ -121,6 +121,31 @@ def test_one_capture_after_another(ctx):
         assert abs(o[0].item() - want) < 1e-6 * want
 
 
+def test_a_captured_step_without_a_number_is_refused(ctx):
+    """The host's count cannot go on in a replay.  With a number, the capture goes on and each replay is that step."""
+    p, g = torch.ones(1000, device="cuda"), torch.full((1000,), 0.5, device="cuda")
+    opt, side, graph = ctx.adamw([p], [g], lr=0.1), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    opt.step()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        for stream in (None, side):
+            with pytest.raises(GbError) as e:
+                opt.step(stream=stream)
+            assert e.value.status == B.GB_ERR_INVALID_ARG and opt.steps == 1
+        opt.step(step=7, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    q = [t.clone() for t in (p, g)]
+    eager = ctx.adamw([q[0]], [q[1]], [opt.exp_avg[0].clone()], [opt.exp_avg_sq[0].clone()], lr=0.1)
+    for _ in range(3):
+        graph.replay()
+        eager.step(step=7)
+    torch.cuda.synchronize()
+    assert torch.equal(p, q[0]) and torch.equal(opt.exp_avg_sq[0], eager.exp_avg_sq[0])
+    opt.step()  # outside of a capture, on from the last number
+    assert opt.steps == 8
+
+
 class DriverStream:
     """A stream that synchronizes with the legacy stream, which torch's streams do not, and its capture."""
 
