@@ -125,9 +125,14 @@ def lib():
     return _lib
 
 
+def _as_it_is(seq):
+    """An array of 64-bit whole numbers: no conversion, of any others one by one."""
+    return isinstance(seq, array) and seq.typecode in "Qq" and len(seq) > 0
+
+
 def _ptrs(seq):
     kind = _vp * max(1, len(seq))
-    if isinstance(seq, array) and seq:  # array("Q"): taken as it is
+    if _as_it_is(seq):
         return kind.from_buffer(seq)
     try:
         return kind(*seq)
@@ -137,7 +142,7 @@ def _ptrs(seq):
 
 def _sizes(seq):
     kind = _sz * max(1, len(seq))
-    if isinstance(seq, array) and seq:
+    if _as_it_is(seq):
         return kind.from_buffer(seq)
     try:
         return kind(*seq)
