@@ -392,7 +392,7 @@ class Context:
         if weight.dim() != 1 or x.dim() < 1 or x.shape[-1] != cols:
             raise GbError(B.GB_ERR_INVALID_ARG, "weight: one dimension, that of x's last")
         n = x.numel()
-        rows = n // cols if cols else 0
+        rows = x.shape[:-1].numel()
         for t, name in ((residual, "residual"), (sum_out, "sum_out")):
             if t is not None and t.numel() != n:
                 raise GbError(B.GB_ERR_INVALID_ARG, "%s: x's size" % name)
@@ -415,7 +415,7 @@ class Context:
         if weight.dim() != 1 or h.dim() < 1 or h.shape[-1] != cols or dweight.numel() != cols:
             raise GbError(B.GB_ERR_INVALID_ARG, "weight and dweight: one dimension, that of h's last")
         n = h.numel()
-        rows = n // cols if cols else 0
+        rows = h.shape[:-1].numel()
         for t, name in ((dy, "dy"), (dx, "dx"), (dsum, "dsum")):
             if t is not None and t.numel() != n:
                 raise GbError(B.GB_ERR_INVALID_ARG, "%s: h's size" % name)

@@ -53,3 +53,24 @@ def test_rms_norm_and_gradient_of_narrow_rows(ctx, cols, dtype):
         assert bool(((cpu64(dx) - want_dx).abs() <= dx_err).all())
         assert bool(((cpu64(dw) - want_dw).abs() <= dw_err).all())
         hold.check()
+
+
+@pytest.mark.parametrize("shape", [(5, 0), (2, 3, 0), (0, 8), (2, 0, 8), (0,), (8,)])
+def test_rms_norm_of_shapes_without_elements(ctx, shape):
+    """No columns, no rows, and a vector of one row: rstd has an entry for every row."""
+    x = torch.ones(shape, device="cuda")
+    w = torch.full(shape[-1:], 2.0, device="cuda")
+    rows = x.shape[:-1].numel()
+    rstd, out, total = torch.full((rows,), 7.0, device="cuda"), torch.zeros_like(x), torch.zeros_like(x)
+    ctx.rms_norm(x, w, out, eps=0.0, residual=x, sum_out=total, rstd=rstd)
+    payload = torch.zeros(rms_norm_payload_bytes("e4m3", 128, rows, shape[-1]), dtype=torch.uint8, device="cuda")
+    ctx.rms_norm(x, w, payload, rstd=rstd, codec="e4m3", block=128)
+    dx, dw = torch.zeros_like(x), torch.full_like(w, 7.0)
+    ctx.rms_norm_backward(x, total, w, rstd, dx, dw)
+    torch.cuda.synchronize()
+    if x.numel():
+        assert bool((out == 2).all()) and bool((total == 2).all()) and bool((rstd - 1 < 1e-5).all())
+    elif shape[-1]:
+        assert bool((dw == 0).all())
+    else:
+        assert bool((rstd == 7).all())  # nothing is written
