@@ -490,7 +490,8 @@ class AdamW:
         """One step, from the gradients as they are now.  step: its number
         (default: one more than the last; a step that the device refuses for
         a grad_scale that is not finite counts too); seed: of the 8-bit
-        states' random numbers.  The number, the seed and the learning rate
+        states' random numbers, another one on each rank that steps shards of
+        its own.  The number, the seed and the learning rate
         are taken at the call: a graph repeats them in every replay, and with
         them the bias correction and the random numbers, so a captured step
         has to be given its number."""

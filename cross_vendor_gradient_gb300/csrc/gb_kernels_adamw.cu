@@ -591,7 +591,9 @@ __global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ AdamwArgs
 constexpr uint32_t kSpanTiles = 32;
 
 // SHIFTED: some tensor of the launch starts off its vectors (in a kernel of
-// its own: the code costs the others registers).
+// its own: the code costs the others registers, and with them a block an SM).
+// 64 tensors of 1 Mi elements, bf16 with copies: 172 us; one of them off its
+// vectors 193 us, half of them 234 us, all 284 us.
 template <typename T, int B, bool COPY, bool SHIFTED, int N>
 __global__ void __launch_bounds__(256, SHIFTED ? 3 : 4) k_adamw8(const __grid_constant__ AdamwArgs<N> a) {
     constexpr int kPer = kTile / B;  // scales of a tile

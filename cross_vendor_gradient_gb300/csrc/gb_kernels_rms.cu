@@ -645,6 +645,10 @@ static cudaError_t rms_launch(RmsArgs &a, cudaStream_t s) {
     constexpr auto kern = k_rms_norm<T, CODEC, B, V, WIDE, SKEW>;
     a.team = team_of(a.cols, V);
     const unsigned threads = a.team >= 32 ? (unsigned)a.team : 256u;
+    // Waves.  Float32: two (16384 x 2048 83 us, 65536 x 768 126; one wave 86
+    // and 128; but 4099 x 769 takes 8.9 us, in one wave 7.9).  16 bits: one
+    // (8192 x 5632 to E4M3 54 us, 4099 x 769 7.8; two waves 55 and 8.9; but
+    // 32768 x 2048 in 16 bits takes 88 us, in two waves 84).
     return launch_pdl(kern, dim3(grid_of<kern>(a.rows, a.team, threads, 0, sizeof(T) == 4 ? 2 : 1)), threads, 0, a, s);
 }
 
@@ -668,7 +672,7 @@ static cudaError_t rms_forward(RmsArgs &a, cudaStream_t s) {
     // leaves no more lanes idle (65536 x 768 to E4M3: 56 us, four 66; 8192 x
     // 5632 to E5M2: 55 us, four 60); two where float32 or a skew needs the
     // registers (16384 x 2048 float32: 83 us, 6.5 TB/s; 2047 columns of bf16:
-    // two 109 us, four 126).
+    // two 105 us, four 130).
     const bool skew = a.cols % 8 != 0;
     if (a.cols <= 249 || a.cols == 256 || (a.rows <= (uint64_t)sm_count() && team_of(a.cols, 1))) return rms_rows<T, CODEC, B, 1>(a, s);
     if ((sizeof(T) == 4 || skew) && team_of(a.cols, 2)) return rms_rows<T, CODEC, B, 2>(a, s);

@@ -634,9 +634,10 @@ typedef struct {
  *   v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m
  *                                 / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * (eps counts as 2^-63 at least: a v of zero next to an m of zero gives no
- * update, whatever eps.)  If *grad_scale (device, read on the stream, such as gb_grad_norm's
- * out + 1) is not finite the step is refused: nothing is written.
+ * (eps counts as 2^-63 at least, and a subnormal v as zero: a v of zero next
+ * to an m of zero gives no update, whatever eps.)  If *grad_scale (device,
+ * read on the stream, such as gb_grad_norm's out + 1) is not finite the step
+ * is refused: nothing is written.
  *   params: float32.  grads: grad_dtype, read only.  copies: NULL, or one
  *   tensor per parameter that receives p rounded to grad_dtype (nearest
  *   even), which must then be BF16 or F16 (GB_ERR_UNSUPPORTED_DTYPE).
@@ -650,10 +651,12 @@ typedef struct {
  *       the distance of E4M3's values around y, the magnitude's code is that
  *       of q floor(|y| / q + r / 65536).  r is a random number of 16 bits
  *       that follows from cfg->seed, cfg->step, t's index and the element's
- *       alone; the seed need not change from step to step.  (To the nearest
- *       code, a moving average whose step is under half of q would stand
- *       still.)  A v of 2^-129 or more is never coded as zero.  Infinities and NaN
- *       are coded as NaN, and leave their block's scale alone.
+ *       alone; the seed need not change from step to step.  Where several
+ *       ranks each call with shards of their own, t counts from 0 on every
+ *       rank: give each rank a seed of its own.  (To the nearest code, a
+ *       moving average whose step is under half of q would stand still.)  A
+ *       v of 2^-129 or more is never coded as zero.  Infinities and NaN are
+ *       coded as NaN, and leave their block's scale alone.
  *     Other codecs: GB_ERR_UNSUPPORTED_CODEC.
  * cfg is read at the call.  A captured call therefore repeats its step in
  * every replay of the graph: the same bias correction, learning rate and
@@ -664,8 +667,10 @@ typedef struct {
  * element only; tensors must not overlap each other.  Streaming at full rate
  * wants all of a tensor's arrays at the same distance, in elements, from a
  * boundary of 8 elements (float32 states), or on one (8-bit states); other
- * tensors take about 1.7 times as long.  Entries of no elements may be NULL.  One launch per 512 tensors; nothing is
- * allocated.  Errors: GB_ERR_INVALID_ARG, GB_ERR_MISALIGNED. */
+ * tensors take 1.7 to 1.9 times as long, and one of them among the up to 512
+ * of a launch with 8-bit states costs the others about a tenth.  Entries of
+ * no elements may be NULL.  One launch per 512 tensors; nothing is allocated.
+ * Errors: GB_ERR_INVALID_ARG, GB_ERR_MISALIGNED. */
 gb_status gb_adamw_step(gb_ctx *ctx, int n_tensors, float *const *params, const void *const *grads,
                         void *const *exp_avg, void *const *exp_avg_sq, void *const *copies, const size_t *numel,
                         gb_dtype grad_dtype, gb_codec state_codec, int block, const gb_adamw *cfg,
@@ -675,7 +680,9 @@ gb_status gb_adamw_step(gb_ctx *ctx, int n_tensors, float *const *params, const 
  * residual's addition.  Per row:
  *   h = x + residual, rounded to dtype (h = x when residual is NULL)
  *   rstd = 1 / sqrt(sum of h^2 / cols + eps)
- *   y = (h rstd) weight
+ *   y = (h weight) rstd
+ * h^2 and its sum are float32 as well: beyond 3.4e38 (elements of 1e19) rstd
+ * is 0, and squares of elements under 1e-23 are 0.
  * sum_out (NULL, or with a residual) receives h, rstd (NULL, or rows floats)
  * the rows' rstd: what gb_rms_norm_backward needs.  out, by codec:
  *   GB_CODEC_NONE: y rounded to dtype;
@@ -684,11 +691,15 @@ gb_status gb_adamw_step(gb_ctx *ctx, int n_tensors, float *const *params, const 
  *     blocks per row (the codec's rule; the last block of a row may be
  *     short): gb_rms_norm_payload_bytes bytes.  With cols a multiple of
  *     block this is a payload of rows * cols elements, which
- *     gb_bridge_decompress_accumulate decodes.  Infinite elements saturate.
+ *     gb_bridge_decompress_accumulate decodes.  A y beyond float32
+ *     saturates; NaN is coded as NaN.
  *   GB_CODEC_BF16: GB_ERR_UNSUPPORTED_CODEC.
- * weight: cols elements.  All element types alike.  Alignment: 16 bytes,
- * an 8-bit out 32, weight its element (a parameter in a packed bucket).  out (GB_CODEC_NONE) or sum_out may be x or residual
- * themselves, not each other; any other overlap is GB_ERR_INVALID_ARG.
+ * An infinite element gives y = NaN in its place (0 times infinity) and 0 in
+ * the rest of its row, a NaN makes the row NaN.
+ * weight: cols elements.  All element types alike.  Alignment: 16 bytes, an
+ * 8-bit out 32, weight its element (a parameter in a packed bucket).  out
+ * (GB_CODEC_NONE) or sum_out may be x or residual themselves, not each other;
+ * any other overlap is GB_ERR_INVALID_ARG.
  * eps must be finite and not negative.  rows == 0 or cols == 0 is a no-op.
  * One launch. */
 size_t gb_rms_norm_payload_bytes(gb_codec codec, int block, size_t rows, size_t cols);
@@ -703,8 +714,9 @@ gb_status gb_rms_norm(gb_ctx *ctx, const void *x, const void *residual, const vo
  *   dweight = sum over the rows of dy xhat
  * rounded to dtype; dweight may lie in a gradient bucket.  With rows == 0
  * dweight is set to zero (the other pointers may be NULL); cols == 0 is a
- * no-op.  Alignment: 16 bytes, weight and dweight their element.  dx may be dy, h or dsum itself; any other
- * overlap is GB_ERR_INVALID_ARG.  cols up to 8 Mi (GB_ERR_TOO_LARGE). */
+ * no-op.  Alignment: 16 bytes, weight and dweight their element.  dx may be
+ * dy, h or dsum itself; any other overlap is GB_ERR_INVALID_ARG.  cols up to
+ * 8 Mi (GB_ERR_TOO_LARGE). */
 gb_status gb_rms_norm_backward(gb_ctx *ctx, const void *dy, const void *h, const void *weight, const float *rstd,
                                const void *dsum, size_t rows, size_t cols, gb_dtype dtype, void *dx, void *dweight,
                                gb_stream stream);

@@ -108,7 +108,7 @@ def check_codes(codes, scales, x, bound, block, words, keep, what):
     assert bool(ok.all()), "%s: scale %r, rule %r" % (what, scales[~ok][0].item(), scale_rule(top)[~ok][0].item())
     s = scales.repeat_interleave(block)[:x.numel()]
     y, dy = x / s, bound / s
-    # as the definition: magnitude q * floor(|y| / q + r); the kernel adds 2^-6 to smaller magnitudes in float32
+    # as the definition: magnitude q * floor(|y| / q + r)
     def at(mag):
         q = quantum(mag)
         z = torch.floor(mag / q + words / 65536) * q
