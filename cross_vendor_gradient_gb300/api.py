@@ -48,7 +48,7 @@ def _capturing(stream):
         return False
     if stream is None:
         return True
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream.cuda_stream)):  # of any kind that has this address
         return torch.cuda.is_current_stream_capturing()
 
 

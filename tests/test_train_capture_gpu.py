@@ -121,6 +121,13 @@ def test_one_capture_after_another(ctx):
         assert abs(o[0].item() - want) < 1e-6 * want
 
 
+class Address:
+    """What a call needs of a stream."""
+
+    def __init__(self, cuda_stream):
+        self.cuda_stream = cuda_stream
+
+
 def test_a_captured_step_without_a_number_is_refused(ctx):
     """The host's count cannot go on in a replay.  With a number, the capture goes on and each replay is that step."""
     p, g = torch.ones(1000, device="cuda"), torch.full((1000,), 0.5, device="cuda")
@@ -129,7 +136,7 @@ def test_a_captured_step_without_a_number_is_refused(ctx):
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
         side.wait_stream(torch.cuda.current_stream())
-        for stream in (None, side):
+        for stream in (None, side, torch.cuda.ExternalStream(side.cuda_stream), Address(side.cuda_stream)):
             with pytest.raises(GbError) as e:
                 opt.step(stream=stream)
             assert e.value.status == B.GB_ERR_INVALID_ARG and opt.steps == 1
